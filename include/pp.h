@@ -316,8 +316,10 @@ PP_API pp_status pp_cache_store(const void *k, const void *v, int64_t k_stride, 
  *   Response i (segment i + g + 1 in group g) has one query, which attends its group's prefix and its own segment, all
  *   lens_d[segment] tokens of each. q: [n_resp, hq, 128] bf16, n_resp = num_segments - num_groups; o the same (it may
  *   be q); lse: [hq, n_resp] fp32 (natural log). A response with no keys gets 0 and -inf. softmax_scale 0 means 1/sqrt(128).
- *   The codes are multiplied exactly; scores, softmax and sums are fp32, and p is rounded to 11 significant bits for
- *   its product with the values. d = 128.
+ *   The codes enter their products exactly. A query row is scaled by a power of two and taken as f16: its bf16 elements
+ *   stay exact, but for those more than 2^14 below the row's largest, which keep what is above 2^-24 of it. Scores,
+ *   softmax and sums are fp32. p times its block's value scale is rounded to 11 significant bits for the product with the
+ *   value codes, and what is below 2^-31 of the largest such product of the row is lost to o (not to lse). d = 128.
  *   workspace: device scratch of ws_bytes >= pp_paged_decode_bytes (host only, from the sizes), 256-byte aligned,
  *   contents need not be initialised. Descriptors or lengths that do not fit yield NaN outputs; a page id outside the
  *   pool yields undefined values in the responses that read it.

@@ -9,6 +9,11 @@
 // Taking log2(sv) into the exponent keeps p_j, which f16 has to hold, at most 2^15 whatever the blocks' scales are:
 // m trails the true maximum by at most 8 and carries an offset of 7, so p reaches down to 2^-31 of its maximum before
 // an f16 loses it (a spike over a long, flat context keeps its tail). L is summed in fp32 from the unrounded p.
+// An f16 keeps 11 bits of p, 2^-12 of it at most off; o is off by some 2^-13 before its own rounding to bf16, which takes
+// up to 2^-8: against 64 bits o is 1.670e-3 off (one response, root mean square, relative) where fp32 throughout gives
+// 1.666e-3, and a few elements in 100 become the other neighbour. With p as two f16 and two products (22 bits) it was 1.666e-3
+// too, at 62.7, 86.5 and 34.8 us where one product takes 58.5, 80.1 and 32.8 (the three large cases below, calls in a row):
+// one is kept.
 //
 // Work: a job is 64 keys of one segment, one kv head and up to 16 query rows: (response, q head) pairs that see the
 // segment, which for a prefix are those of all the group's responses. Jobs lie in the order (segment, head, rows,
