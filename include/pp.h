@@ -298,9 +298,11 @@ PP_API pp_status pp_pages_resize(const int32_t *group_start_d, int32_t num_group
 
 /* pp_cache_store: round rows of keys and values to 8 bits and write them at their slots.
  *   k, v: n rows of [hkv, 128] in dt (PP_BF16 or PP_FP32), k_stride and v_stride elements apart (a multiple of 16
- *   bytes); slots_d: int32 [n], a negative slot skips its row. The rows of one page stand together in ascending
- *   order of slot, as pp_pages_resize gives them (a page that appears in two places of one call is written in no
- *   defined order). A row at offset 0 starts its page anew; rows that begin at offset o keep the o tokens before them.
+ *   bytes); slots_d: int32 [n], a negative slot skips its row. The rows of one page stand together, as pp_pages_resize
+ *   gives them: each within 256 rows of the one before, skipped rows between them and none of another page. Their slots
+ *   may leave gaps and come in any order; of two rows with one slot the later stands (both count for the scale). A page in
+ *   two places of one call is written in no defined order. Rows whose smallest offset is 0 start their page anew; with a
+ *   smallest offset o they keep the o tokens before it. Codes past o that no row names stay, but stand for nothing.
  *   The scale of a (page, head) block is the smallest 2^e, -40 <= e <= 56, under which its largest finite value does
  *   not exceed the largest code (448 for e4m3, 127 for int8), or the block's scale so far if that is larger; when it
  *   grows, the codes of the tokens before are rounded again. Codes round to nearest even; values beyond the largest

@@ -334,7 +334,8 @@ def pp_pages_resize(group_start_d, seg_group_d, old_lens_d, new_lens_d, page_siz
 
 def pp_cache_store(k, v, slots_d, k_pages, v_pages, k_scale, v_scale, stream=None):
     """Append rows k, v [n, hkv, d] at their slots: k_pages [num_pages, hkv, page_size, d], v_pages [num_pages, hkv, d,
-    page_size] (float8_e4m3fn or int8), k_scale, v_scale fp32 [num_pages, hkv]."""
+    page_size] (float8_e4m3fn or int8), k_scale, v_scale fp32 [num_pages, hkv]. The rows of one page stand together: each
+    within 256 rows of the one before, skipped rows (slot -1) between them and none of another page."""
     _done("pp_cache_store", _bind().cache_store(k, v, slots_d, k_pages, v_pages, k_scale, v_scale, stream))
 
 

@@ -8,7 +8,8 @@
 // its codes lose their last bits. Codes of e4m3 keep 4 significant bits whatever e is, so the power of two costs them
 // nothing in range or precision; int8 gives up at most one of its 8 bits.
 //
-// Appending to a page that already holds tokens keeps the larger of its scale and the one that the new rows need; if
+// The rows of one page that stand together in a call are one append, whatever the order and the gaps of their slots: one
+// owner forms their one scale. Appending to a page that already holds tokens keeps the larger of its scale and the one that the new rows need; if
 // it grows, the codes already there are re-rounded to it. Values that are not finite do not count for the scale.
 #pragma once
 #include <cuda_bf16.h>
@@ -28,6 +29,7 @@ constexpr int CACHE_THREADS = 256;
 // to 4 rows 7.5, 7.4, 9.9, 15.7 and 14.5, 18.8, 38.3, 52.6 us; up to 8 rows (longer code, more registers) 8.6, 8.9, 12.2,
 // 20.3 and 17.4, 23.1, 40.9, 53.6; single rows only 7.1, 11.9, 12.5, 15.8 and 14.3, 35.0, 48.1, 52.4.
 constexpr int CACHE_SHORT = 4;
+constexpr int CACHE_APART = 256;      // rows of a page are one append if each is at most this many rows after the one before
 
 enum CacheFmt : int { CACHE_E4M3 = 0, CACHE_INT8 = 1 };
 
@@ -143,10 +145,172 @@ __device__ __forceinline__ void cache_rescale(uint8_t *blk, bool val, int page, 
     }
 }
 
+// 1 + the rows after i that go on with its run (at most a page).
+__device__ __forceinline__ int cache_run_len(const uint32_t *cont, int i) {
+    int j = i + 1;
+    while (j < 256) {
+        const uint32_t w = cont[j >> 5] >> (j & 31);
+        const int ones = ~w ? __ffs(~w) - 1 : 32;
+        const int room = 32 - (j & 31);
+        j += min(ones, room);
+        if (ones < room) break;
+    }
+    return j - i;
+}
+
+// The long look at the slots, for windows whose rows may stand apart: from row w0 - CACHE_THREADS on; bits of slots from there,
+// and of the rows from w0 on that belong to the append of the last row with a slot before them.
+constexpr int CACHE_LOOK = 2 * CACHE_THREADS;         // from w0 on: a window, a page's run after it and CACHE_APART more
+static_assert(CACHE_LOOK >= 2 * 128 + CACHE_APART && CACHE_APART <= CACHE_THREADS, "rows looked at");
+struct CacheLook {
+    int32_t slot[CACHE_THREADS + CACHE_LOOK];         // -1: a row without one
+    uint32_t valid[(CACHE_THREADS + CACHE_LOOK) / 32], join[CACHE_LOOK / 32];
+};
+// Sets `head` to the rows of the window that begin an append of one run, `apart` to those whose append has more rows. For the
+// whole block.
+static __device__ __noinline__ void cache_look_apart(const int32_t *slots, int64_t n, int64_t w0, int window, int lg, int64_t limit,
+                                                     const uint32_t *cont, uint32_t *head, uint32_t *apart, CacheLook &k) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int W = CACHE_THREADS / 32;
+    for (int z = 0; z < 3; ++z) {
+        const int64_t i = w0 + tid + (z - 1) * CACHE_THREADS;
+        int32_t slot = i >= 0 && i < n ? slots[i] : -1;
+        if (slot >= limit) slot = -1;
+        k.slot[z * CACHE_THREADS + tid] = slot;
+        const uint32_t bv = __ballot_sync(0xffffffffu, slot >= 0);
+        if (lane == 0) k.valid[z * W + warp] = bv;
+    }
+    __syncthreads();
+    bool begins = false;
+    for (int z = 0; z < 2; ++z) {
+        const int r = (z + 1) * CACHE_THREADS + tid;  // in k.slot
+        const int32_t slot = k.slot[r];
+        bool join = false;
+        if (slot >= 0) {
+            int p = r - 1;                            // the last row with a slot, if it is near enough
+            while (p >= r - CACHE_APART && k.slot[p] < 0) {
+                const uint32_t w = k.valid[p >> 5] << (31 - (p & 31));
+                p = w ? p - __clz(w) : (p & ~31) - 1;
+            }
+            join = p >= r - CACHE_APART && k.slot[p] >> lg == slot >> lg;
+        }
+        const uint32_t bj = __ballot_sync(0xffffffffu, join);
+        if (lane == 0) k.join[z * W + warp] = bj;
+        if (z == 0) begins = slot >= 0 && !join && tid < window;
+    }
+    __syncthreads();
+    bool more = false;
+    if (begins) {                                     // does the next row with a slot join its first run?
+        const int from = tid + cache_run_len(cont, tid);
+        for (int j = from, end = min(CACHE_LOOK, from + CACHE_APART); j < end; j = (j | 31) + 1) {
+            const uint32_t w = k.valid[W + (j >> 5)] >> (j & 31);
+            if (w) {
+                const int next = j + __ffs(w) - 1;
+                more = k.join[next >> 5] >> (next & 31) & 1;
+                break;
+            }
+        }
+    }
+    const uint32_t bb = __ballot_sync(0xffffffffu, begins && !more), bm = __ballot_sync(0xffffffffu, more);
+    if (lane == 0 && warp < 4) {
+        head[warp] = bb;
+        apart[warp] = bm;
+    }
+    __syncthreads();
+}
+
+// A page's rows that are not one run: from row i0 on, skipped rows and rows in any order among them, up to the last that
+// follows the one before within CACHE_APART rows with no other page's row between. The whole block, a warp a row, each row
+// read twice: no caller of pp_pages_resize has such rows. s_row: 128 ints, s_red: 8 words, both free on entry.
+template <typename T, int FMT>
+static __device__ __noinline__ void cache_store_apart(const T *rows, int64_t stride, const int32_t *slots, int64_t n, int64_t i0, int lg,
+                                                      int32_t num_pages, int hkv, bool val, int h0, int h1, uint8_t *pages,
+                                                      float *scales, int32_t *s_row, uint32_t *s_red) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int page = 1 << lg;
+    const int32_t pg = slots[i0] >> lg;
+    const int64_t limit = int64_t(num_pages) << lg;
+    auto slot_of = [&](int64_t i) {                       // of a row of any page, else -1
+        const int32_t s = i < n ? slots[i] : -1;
+        return s < limit ? s : -1;
+    };
+    int64_t last = i0;                                    // the same for all threads
+    for (int64_t base = i0 + 1; base < n && base - last <= CACHE_APART; base += 32) {
+        const int32_t s = slot_of(base + lane);           // every warp for itself: 32 rows at a time
+        const uint32_t other = __ballot_sync(0xffffffffu, s >= 0 && s >> lg != pg);
+        uint32_t same = __ballot_sync(0xffffffffu, s >= 0 && s >> lg == pg);
+        if (other) same &= (other & (0u - other)) - 1;    // those before the first other
+        bool end = other != 0;
+        for (; same; same &= same - 1) {
+            const int64_t i = base + __ffs(same) - 1;
+            if (i - last > CACHE_APART) {
+                end = true;
+                break;
+            }
+            last = i;
+        }
+        if (end) break;
+    }
+    const int64_t len = last - i0 + 1;
+    rows += i0 * stride;
+    // the row of each place; of a slot that is named twice, the last
+    __syncthreads();
+    if (tid < page) s_row[tid] = -1;
+    __syncthreads();
+    for (int64_t t = tid; t < len; t += CACHE_THREADS) {
+        const int32_t s = slot_of(i0 + t);
+        if (s >= 0) atomicMax(&s_row[s & (page - 1)], int32_t(t));
+    }
+    __syncthreads();
+    int o0 = 0;
+    while (s_row[o0] < 0) ++o0;                           // row i0 has one
+    auto load = [&](int64_t t, int h, float (&x)[4]) {    // a lane four elements
+        const T *row = rows + t * stride + h * CACHE_D + 4 * lane;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = static_cast<float>(row[e]);
+    };
+#pragma unroll 1
+    for (int h = h0; h < h1; ++h) {
+        const int64_t at = int64_t(pg) * hkv + h;
+        uint8_t *blk = pages + (at << lg) * CACHE_D;
+        const float old = o0 > 0 ? scales[at] : 0.f;
+        float amax = 0.f;
+#pragma unroll 1
+        for (int64_t t = warp; t < len; t += CACHE_THREADS / 32)
+            if (slot_of(i0 + t) >= 0) {
+                float x[4];
+                load(t, h, x);
+                for (int e = 0; e < 4; ++e) amax = fmaxf(amax, finite_abs(x[e]));
+            }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        if (lane == 0) s_red[warp] = __float_as_uint(amax);
+        __syncthreads();
+        for (int k = 0; k < CACHE_THREADS / 32; ++k) amax = fmaxf(amax, __uint_as_float(s_red[k]));
+        const float sc = fmaxf(old, cache_scale<FMT>(amax)), inv = 1.f / sc;
+        if (o0 > 0 && sc > old) cache_rescale<FMT>(blk, val, page, o0, old * inv, tid, CACHE_THREADS);
+        if (tid == 0) scales[at] = sc;
+        __syncthreads();                                  // the re-rounded words are written before the new bytes
+#pragma unroll 1
+        for (int o = o0 + warp; o < page; o += CACHE_THREADS / 32) {
+            const int32_t t = s_row[o];
+            if (t < 0) continue;
+            float x[4];
+            load(t, h, x);
+            const uint32_t w = cache_code4<FMT>(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+            if (!val) reinterpret_cast<uint32_t *>(blk + o * CACHE_D)[lane] = w;
+            else
+                for (int e = 0; e < 4; ++e) blk[(4 * lane + e) * page + o] = uint8_t(w >> (8 * e));
+        }
+    }
+    __syncthreads();
+}
+
 // grid windows * parts, a window's blocks next to each other so that its rows' heads are read at about the same time: a
-// block takes the runs that begin in its window of rows, for some heads' keys (even part) or values (odd). A run is a
-// stretch of rows whose slots ascend by one within a page: the rows of one (page, head) block, which one block or warp
-// therefore owns. Runs of up to CACHE_SHORT rows (an appended token) go to a warp each; longer ones to the whole block,
+// block takes the appends that begin in its window of rows, for some heads' keys (even part) or values (odd). An append
+// is all rows of one page that stand together, skipped rows among them: those of one (page, head) block, which one block
+// or warp therefore owns. Nearly always it is a run, slots that ascend by one row by row; what is not goes to
+// cache_store_apart. Runs of up to CACHE_SHORT rows (an appended token) go to a warp each; longer ones to the whole block,
 // rows held in registers between the maximum and the codes, so that every row is read once, and the next head's rows
 // asked for before this one's codes are written. A decode step (128 rows of 8 heads, 6.1 us) is bound by latency: slots,
 // rows and scale, codes. A prefill (88,685 bf16 rows of 8 heads, 545 MB read and written in 122 us: 4.5 TB/s, 68 % of a
@@ -160,7 +324,8 @@ __global__ void __launch_bounds__(CACHE_THREADS, UNITS == 1 ? 4 : UNITS == 2 ? 3
     using V = typename RV::V;
     constexpr int N = RV::N, VR = CACHE_D / N;        // elements of a vector, vectors of a row
     constexpr int MAX_PAGE = 128;
-    __shared__ uint32_t s_cont[8], s_head[4];
+    static_assert(sizeof(CacheLook) <= sizeof(uint32_t) * 2 * CACHE_D * (MAX_PAGE / 4 + 1), "a look fits s_v");
+    __shared__ uint32_t s_cont[8], s_head[4], s_apart[4];
     __shared__ float s_max[2][CACHE_THREADS / 32], s_wild[CACHE_THREADS / 32];
     __shared__ uint32_t s_v[2][CACHE_D][MAX_PAGE / 4 + 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -174,31 +339,28 @@ __global__ void __launch_bounds__(CACHE_THREADS, UNITS == 1 ? 4 : UNITS == 2 ? 3
     float *scales = val ? a.scale[1] : a.scale[0];
     const int64_t w0 = int64_t(window) * a.window;
     const int64_t limit = int64_t(a.num_pages) << lg;
-    {   // bit i of s_cont: row w0 + i goes on with the run of the row before it; of s_head: a run begins there
+    bool odd;                                         // rows of a page may stand apart
+    {   // bit i of s_cont: row w0 + i goes on with the run of the row before it; of s_head: an append begins there
         const int64_t i = w0 + tid;
         const int32_t slot = i < a.n ? a.slots[i] : -1, before = i > 0 && i < a.n ? a.slots[i - 1] : -1;
-        const bool valid = slot >= 0 && slot < limit;
-        const bool cont = valid && before >= 0 && slot == before + 1 && (slot & (page - 1)) != 0;
+        const bool valid = slot >= 0 && slot < limit, known = before >= 0 && before < limit;
+        const bool same = valid && known && before >> lg == slot >> lg, cont = same && slot == before + 1;
         const uint32_t bc = __ballot_sync(0xffffffffu, cont);
         const uint32_t bh = __ballot_sync(0xffffffffu, valid && !cont && tid < a.window);
         if (lane == 0) {
             s_cont[warp] = bc;
-            if (warp < 4) s_head[warp] = bh;
+            if (warp < 4) {
+                s_head[warp] = bh;
+                s_apart[warp] = 0;
+            }
         }
         if (slot >= limit && tid < a.window && h0 == 0 && !val) set_dev_err(DEVERR_BAD_PAGES);
+        // a row after a skipped one, or in its page but not the next; or skipped rows to the end of the look
+        odd = valid ? i > 0 && (!known || (same && !cont)) : tid == CACHE_THREADS - 1 && i < a.n;
     }
-    __syncthreads();
-    auto run_len = [&](int i) {                       // 1 + the continuing rows after i (at most a page)
-        int j = i + 1;
-        while (j < 256) {
-            const uint32_t w = s_cont[j >> 5] >> (j & 31);
-            const int ones = ~w ? __ffs(~w) - 1 : 32;
-            const int room = 32 - (j & 31);
-            j += min(ones, room);
-            if (ones < room) break;
-        }
-        return j - i;
-    };
+    if (__syncthreads_or(odd))
+        cache_look_apart(a.slots, a.n, w0, a.window, lg, limit, s_cont, s_head, s_apart, *reinterpret_cast<CacheLook *>(s_v));
+    auto run_len = [&](int i) { return cache_run_len(s_cont, i); };
     // ---- short runs: one warp each, a lane four elements of every row
     int ord = 0;
     for (int wd = 0; wd < (a.window + 31) / 32; ++wd) {
@@ -386,6 +548,13 @@ __global__ void __launch_bounds__(CACHE_THREADS, UNITS == 1 ? 4 : UNITS == 2 ? 3
                 }
             }
         }
+    }
+    if (s_apart[0] | s_apart[1] | s_apart[2] | s_apart[3]) {
+        __syncthreads();                              // s_v is no longer read
+        for (int wd = 0; wd < 4; ++wd)
+            for (uint32_t b = s_apart[wd]; b; b &= b - 1)
+                cache_store_apart<T, FMT>(rows, stride, a.slots, a.n, w0 + wd * 32 + __ffs(b) - 1, lg, a.num_pages, a.hkv, val, h0, h1,
+                                          pages, scales, reinterpret_cast<int32_t *>(s_v[0][0]), reinterpret_cast<uint32_t *>(s_wild));
     }
 }
 

@@ -73,7 +73,9 @@ class PagedCache:
         return slots, pos, counts
 
     def append(self, k, v, slots, stream=None):
-        """Round the rows k, v [n, hkv, d] (bf16 or fp32) to 8 bits and write them at slots [n]."""
+        """Round the rows k, v [n, hkv, d] (bf16 or fp32) to 8 bits and write them at slots [n] (-1 skips a row). Slots
+        as ``resize`` gives them; others need the rows of one page to stand together: each within 256 rows of the one
+        before, with skipped rows between them and none of another page."""
         _lib.pp_cache_store(k, v, slots, self.k_pages, self.v_pages, self.k_scale, self.v_scale, stream)
 
     def decode(self, q, softmax_scale: float = 0.0, out=None, lse=None, stream=None):

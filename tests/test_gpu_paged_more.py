@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from tests.paged_util import random_cache
+from tests.test_gpu_paged import _store_both
 
 pytestmark = pytest.mark.gpu
 
@@ -44,3 +45,61 @@ def test_decode_repeats_bit_for_bit(num, lens, heads, page, codes):
         pp.pp_paged_decode(*a)
         assert torch.equal(a[9], o) and torch.equal(a[10], lse)
     pp.pp_get_status()
+
+
+# ------------------------------------------------------------------------------------------------------------- append
+def _rows(rng, n, heads, dtype):
+    """Rows of far-apart sizes, so that each decides a scale of its own."""
+    size = np.exp(rng.uniform(-6, 6, (n, heads, 1)))
+    return [torch.from_numpy(rng.standard_normal((n, heads, 128)) * size).to(dtype).cuda() for _ in range(2)]
+
+
+APART = {                                                    # slots of page 1, as offsets; None skips a row
+    "a gap": [3, 5],
+    "a gap from the start": [0, 1, 3, 4],
+    "a skipped row": [3, None, 4],
+    "skipped rows and gaps": [1, None, None, 4, 5, 6, 7, 8, 9, None, 12],
+    "descending": [9, 7, 3, 2],
+    "the smallest last": [5, 6, 7, 8, 9, 10, 0],
+    "twice": [4, 4, 6, 5, 6],
+    "as far apart as may be": [2] + [None] * 255 + [3, 9],
+    "again and again": ([2] + [None] * 200) * 3 + [8, 9, 10, 11, 12, 13],
+}
+
+
+@pytest.mark.parametrize("dtype,page,codes", [(torch.bfloat16, 16, "e4m3"), (torch.float32, 64, "int8"), (torch.bfloat16, 128, "int8")])
+@pytest.mark.parametrize("what", list(APART))
+def test_store_rows_of_a_page_apart(what, dtype, page, codes):
+    """Rows of one page with gaps between their slots, skipped rows between them, or in another order are one append: one
+    scale over all of them, alone in a call, behind other pages' rows, and where a block's window of 8 rows ends."""
+    rng = np.random.default_rng(len(what))
+    mine = [-1 if o is None else page + o for o in APART[what]]
+    for before in ([], [0, 1, 2, 3, 4], [page * 3 + page - 1, -1, -1, 2 * page, 2 * page + 1]):
+        slots = before + mine + [-1, 4 * page, 4 * page + 1, 4 * page + 2]
+        _store_both(*_rows(rng, len(slots), 3, dtype), slots, page, 5, codes, 3)
+
+
+@pytest.mark.parametrize("dtype,page,codes", [(torch.bfloat16, 16, "int8"), (torch.bfloat16, 64, "e4m3"), (torch.float32, 32, "e4m3"),
+                                              (torch.bfloat16, 128, "e4m3")])
+def test_store_many_rows_apart(dtype, page, codes):
+    """Enough rows for windows of a page: whole pages, runs and pages with gaps, their rows across the windows' ends,
+    stretches of skipped rows, and the end of a call inside a page."""
+    rng = np.random.default_rng(page)
+    slots, num_pages = [], 4000 // page + 200
+    for pg in rng.permutation(num_pages):
+        if len(slots) > 4000:
+            break
+        first = int(rng.integers(0, page)) if rng.random() < 0.5 else 0
+        take = np.arange(first, int(rng.integers(first, page)) + 1)
+        kind = rng.integers(0, 4)
+        if kind == 1:
+            take = take[rng.random(len(take)) < 0.7]
+        if kind == 2:
+            take = rng.permutation(take)
+        for o in take:
+            slots.append(int(pg) * page + int(o))
+            if kind == 3 and rng.random() < 0.2:
+                slots += [-1] * int(rng.integers(1, 4))
+        if rng.random() < 0.1:
+            slots += [-1] * int(rng.integers(1, 400))
+    _store_both(*_rows(rng, len(slots), 3, dtype), slots, page, num_pages, codes, 5)
