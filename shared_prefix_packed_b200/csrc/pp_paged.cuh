@@ -256,7 +256,7 @@ template <int NB> struct PagedItem {
     float cq[NB][2], m[NB][2], l[NB][2];
 };
 
-// Query row n of a job as f16, scaled to [1, 2): a lane 32 elements from 32 (lane % 4) on; and the factor that takes its
+// Query row n of a job as f16, scaled to [1, 2) (the largest and smallest rows to [2^-6, 4)): a lane 32 elements from 32 (lane % 4) on; and the factor that takes its
 // products back to exponents. Rows past the last are zeros.
 struct PagedRow {
     uint32_t q[16];
@@ -280,9 +280,9 @@ static __device__ __noinline__ PagedRow paged_row_f16(const PagedArgs &a, const 
     for (int i = 0; i < 16; ++i) mx = fmax3(mx, fabsf(bf16lo(x[i])), fabsf(bf16hi(x[i])));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    // e = 0 for a row of zeros or with an infinity or NaN, which f16 keeps
+    // e = 0 for a row of zeros or with an infinity or NaN, which f16 keeps; at most 126, so that 2^-e is a normal number
     int e2 = int(__float_as_uint(mx) >> 23) - 127;
-    e2 = mx == 0.f || e2 == 128 ? 0 : max(e2, -120);
+    e2 = mx == 0.f || e2 == 128 ? 0 : min(max(e2, -120), 126);
     const float down = __uint_as_float(uint32_t(127 - e2) << 23);
     PagedRow out;
 #pragma unroll

@@ -4,7 +4,8 @@ import numpy as np
 import pytest
 import torch
 
-from tests.paged_util import random_cache
+from oracle import paged_cache as pc
+from tests.paged_util import decode_bounds, random_cache
 from tests.test_gpu_paged import _store_both
 
 pytestmark = pytest.mark.gpu
@@ -21,6 +22,12 @@ def _decode_args(c, hq, seed, q=None):
     ws = torch.empty(pp.pp_paged_decode_bytes(n, hq, sk.shape[1]), dtype=torch.uint8, device="cuda")
     return [q.cuda(), d["k"], d["v"], sk, sv, d["start"], d["seg_group"], d["lens_t"], d["table_t"],
             torch.empty(n, hq, 128, dtype=torch.bfloat16, device="cuda"), torch.empty(hq, n, device="cuda"), ws]
+
+
+def _call_decode(a):
+    import shared_prefix_packed_b200 as pp
+    pp.pp_paged_decode(*a)
+    pp.pp_get_status()
 
 
 @pytest.mark.parametrize("num,lens,heads,page,codes", [
@@ -45,6 +52,27 @@ def test_decode_repeats_bit_for_bit(num, lens, heads, page, codes):
         pp.pp_paged_decode(*a)
         assert torch.equal(a[9], o) and torch.equal(a[10], lse)
     pp.pp_get_status()
+
+
+@pytest.mark.parametrize("top,k_exp", [(127, -126), (126, -126), (125, -124), (-120, 118), (-126, 120)])
+def test_decode_queries_at_the_ends_of_bf16(top, k_exp):
+    """Rows whose largest |q| lies in [2^top, 2^(top + 1)), with key scales that make their scores ordinary."""
+    num, lens, page, hq, hkv = [2, 1], [40, 10, 20, 5, 130], 32, 4, 2
+    c = random_cache(num, lens, page, hkv, "e4m3", 9)
+    c["k_scale"][:] = 2.0 ** k_exp
+    x = np.random.default_rng(3).standard_normal((3, hq, 128)) / 4
+    x = np.where(np.abs(x) < 2.0 ** -6, 0, x)                # no element that f16 would lose bits of
+    x[:, :, 7] = 1.9
+    q = torch.from_numpy(x * 2.0 ** top).to(torch.bfloat16)
+    assert torch.isfinite(q.float()).all()
+    a = _decode_args(c, hq, 0, q)
+    _call_decode(a)
+    want = pc.decode(q.double().numpy(), c["k_vals"], c["v_vals"], c["k_scale"].astype(np.float64),
+                     c["v_scale"].astype(np.float64), num, lens, c["table"])
+    assert 1 < np.abs(want[3]).max() < 1e4
+    bo, bl = decode_bounds(*want, n_keys=sum(lens), scale_exp=7)
+    assert np.all(np.abs(a[9].double().cpu().numpy() - want[0]) <= bo)
+    assert np.all(np.abs(a[10].double().cpu().numpy() - want[1]) <= bl)
 
 
 # ------------------------------------------------------------------------------------------------------------- append
