@@ -286,8 +286,10 @@ PP_API pp_status pp_qk_norm_rope_bwd(const void *q, const void *k, int64_t q_str
  *   grouped position (place in a prefix; the prefix's new length plus its place in a response). Entries past the last
  *   new token get slot -1 (which pp_cache_store skips) and position 0. counts_d: int32 [4] out: new tokens, pages
  *   taken, pages given back, and 1.
- *   Where the pool has too few pages, the new tokens exceed `capacity`, or a length is negative or exceeds
- *   max_pages * page_size, nothing changes: counts are {0, 0, 0, 0}, every slot -1, *n_free_out = *n_free_in.
+ *   Where the pool has too few pages, the new tokens exceed `capacity`, a length is negative or exceeds
+ *   max_pages * page_size, or a page to be given back is none of the pool's, nothing changes: counts are {0, 0, 0, 0},
+ *   every slot -1, *n_free_out = *n_free_in. A free page, or a growing segment's last page, that is none of the pool's is
+ *   reported too, but the change stands: its tokens get slot -1.
  *   max_pages * page_size <= 2^30; num_pages * page_size < 2^31.
  */
 PP_API pp_status pp_pages_resize(const int32_t *group_start_d, int32_t num_groups, const int32_t *seg_group_d,

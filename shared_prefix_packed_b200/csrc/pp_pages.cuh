@@ -10,8 +10,9 @@
 // One launch of one cluster of 8 CTAs, bound by latency: every CTA scans the segments for itself (three running
 // counts in shared memory), so nothing is passed between CTAs but the free list, and the cluster barrier stands
 // between pages given back and pages taken. A step of 144 segments takes 7.7 us (with one CTA 7.9), a prefill that maps
-// 147,786 tokens 15.5 (with one CTA 64). A count that does not fit is seen by every CTA alike before any write, so
-// the call changes everything or nothing.
+// 147,786 tokens 15.5 (with one CTA 64). A count that does not fit is seen by every CTA alike before any write, and so is a
+// page id outside the pool among those given back (one more cluster barrier in calls that give pages back), so the call
+// changes everything or nothing.
 #pragma once
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
@@ -48,7 +49,7 @@ __global__ void __launch_bounds__(PAGES_THREADS) k_pages_resize(const PagesArgs 
     int32_t *tok = sh, *need = sh + (a.nseg + 1), *back = sh + 2 * (a.nseg + 1);
     __shared__ int32_t s_tmp[3 * 32];
     __shared__ unsigned long long s_tok, s_need, s_back;
-    __shared__ int s_bad;
+    __shared__ int s_bad, s_out;
     const int tid = threadIdx.x, lg = a.page_log2, page = 1 << lg;
     if (tid == 0) {
         s_tok = s_need = s_back = 0;
@@ -86,25 +87,41 @@ __global__ void __launch_bounds__(PAGES_THREADS) k_pages_resize(const PagesArgs 
     if (tid == 0) tok[a.nseg] = need[a.nseg] = back[a.nseg] = 0;
     __syncthreads();
     // 64-bit totals, so a sum past 2^31 is refused rather than wrapped
-    const bool ok = !s_bad && n_free >= 0 && n_free <= a.num_pages && s_tok <= (unsigned long long)a.room &&
+    bool ok = !s_bad && n_free >= 0 && n_free <= a.num_pages && s_tok <= (unsigned long long)a.room &&
                     s_back <= (unsigned long long)(a.num_pages - n_free) &&
                     s_need <= (unsigned long long)n_free + s_back;
     const int64_t nthreads = int64_t(cluster.num_blocks()) * PAGES_THREADS;
     const int64_t me = int64_t(cluster.block_rank()) * PAGES_THREADS + tid;
-    const int32_t R = ok ? int32_t(s_back) : 0, K = ok ? int32_t(s_need) : 0, NT = ok ? int32_t(s_tok) : 0;
+    int32_t R = ok ? int32_t(s_back) : 0, K = ok ? int32_t(s_need) : 0, NT = ok ? int32_t(s_tok) : 0;
+    auto given = [&](int64_t i) {                        // the i-th page given back
+        const int s = seg_of(back, a.nseg, int32_t(i));
+        const int32_t n = a.new_lens[s];
+        const int64_t at = int64_t(n >> lg) + ((n & (page - 1)) != 0) + (i - back[s]);
+        return a.table[s * a.max_pages + at];
+    };
     if (ok) {
         int32_t *const arrs[3] = {tok, need, back};
         int32_t tots[3];
         block_exclusive_scan_multi<PAGES_THREADS, 3>(arrs, a.nseg + 1, s_tmp, tots);
         __syncthreads();
-        for (int64_t i = me; i < R; i += nthreads) {
-            const int s = seg_of(back, a.nseg, int32_t(i));
-            const int32_t n = a.new_lens[s];
-            const int64_t at = int64_t(n >> lg) + ((n & (page - 1)) != 0) + (i - back[s]);
-            a.free_pages[n_free + i] = a.table[s * a.max_pages + at];
+        if (R > 0) {                                     // the same for all CTAs
+            bool out = false;
+            for (int64_t i = me; i < R; i += nthreads) {
+                const int32_t id = given(i);
+                out |= id < 0 || id >= a.num_pages;
+            }
+            out = __syncthreads_or(out);
+            if (tid == 0) s_out = out;
+            cluster.sync();
+            for (unsigned r = 0; r < cluster.num_blocks(); ++r) out |= *cluster.map_shared_rank(&s_out, r) != 0;
+            if (out) {
+                ok = false;
+                R = K = NT = 0;
+            }
         }
+        for (int64_t i = me; i < R; i += nthreads) a.free_pages[n_free + i] = given(i);
     }
-    cluster.sync();                                      // n_free is read and the pages given back are listed
+    cluster.sync();                                      // n_free and s_out are read and the pages given back are listed
     if (me == 0) {
         *a.n_free_out = n_free + R - K;
         a.counts[0] = NT;

@@ -131,3 +131,49 @@ def test_store_many_rows_apart(dtype, page, codes):
         if rng.random() < 0.1:
             slots += [-1] * int(rng.integers(1, 400))
     _store_both(*_rows(rng, len(slots), 3, dtype), slots, page, num_pages, codes, 5)
+
+
+# ------------------------------------------------------------------------------------------------------------- resize
+def _resize_args(old, new, table, free, n_free, page, capacity):
+    t = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    n = t([n_free])
+    return [t([0, len(old)]), t([0] * len(old)), t(old), t(new), page, t(table), t(free), n, n, t([9] * capacity), t([9] * capacity), t([9] * 4)]
+
+
+@pytest.mark.parametrize("bad", [-1, 12, 2 ** 31 - 1, -2 ** 31])
+@pytest.mark.parametrize("new", [[3, 0, 20], [3, 0, 60], [3, 16, 20]])
+def test_resize_refuses_to_take_back_pages_outside_the_pool(new, bad):
+    """A shrinking segment whose row names a page that the pool does not have: nothing changes, and it is reported."""
+    import shared_prefix_packed_b200 as pp
+    old, table, free = [3, 40, 20], [[0, -1, -1, -1], [1, 2, bad, -1], [3, 4, -1, -1]], [5, 6, 7, 8, 9, 10, 11, -5, -5, -5, -5, -5]
+    a = _resize_args(old, new, table, free, 7, 16, 50)
+    pp.pp_pages_resize(*a)
+    with pytest.raises(pp.PPError, match="cache pages"):
+        pp.pp_get_status()
+    assert a[11].tolist() == [0] * 4 and a[8].tolist() == [7] and (a[9] == -1).all() and (a[10] == 0).all()
+    assert a[5].tolist() == table and a[6].tolist() == free
+    a[5][1, 2] = 11                                          # (and no longer on the free list)
+    a[7].fill_(6)
+    pp.pp_pages_resize(*a)                                   # the next call, with a row that fits, is made
+    assert a[11].tolist()[3] == 1
+    pp.pp_get_status()
+
+
+@pytest.mark.parametrize("at", [None, 0, 1023, 1024, 5000, 8999])
+def test_resize_takes_back_many_pages_or_none(at):
+    """9,000 pages given back, more than one CTA of the cluster looks at: all or, with one that does not fit, none."""
+    import shared_prefix_packed_b200 as pp
+    table = np.random.default_rng(3).permutation(9000).reshape(3000, 3)
+    if at is not None:
+        table[at // 3, at % 3] = 9000
+    free = [-7] * 9000
+    a = _resize_args([40] * 3000, [0] * 3000, table.tolist(), free, 0, 16, 5)
+    pp.pp_pages_resize(*a)
+    if at is None:
+        pp.pp_get_status()
+        assert a[11].tolist() == [0, 0, 9000, 1] and a[6].tolist() == table.reshape(-1).tolist() and a[8].item() == 9000
+    else:
+        with pytest.raises(pp.PPError, match="cache pages"):
+            pp.pp_get_status()
+        assert a[11].tolist() == [0] * 4 and a[6].tolist() == free and a[8].item() == 0
+    assert a[5].tolist() == table.tolist()
