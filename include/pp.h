@@ -288,7 +288,8 @@ PP_API pp_status pp_qk_norm_rope_bwd(const void *q, const void *k, int64_t q_str
  *   taken, pages given back, and 1.
  *   Where the pool has too few pages, the new tokens exceed `capacity`, a length is negative or exceeds
  *   max_pages * page_size, or a page to be given back is none of the pool's, nothing changes: counts are {0, 0, 0, 0},
- *   every slot -1, *n_free_out = *n_free_in. A free page, or a growing segment's last page, that is none of the pool's is
+ *   every slot -1, *n_free_out = *n_free_in, and pp_get_status reports it, the first two, which a server may meet at any
+ *   time, by a message of their own. A free page, or a growing segment's last page, that is none of the pool's is
  *   reported too, but the change stands: its tokens get slot -1.
  *   max_pages * page_size <= 2^30; num_pages * page_size < 2^31.
  */

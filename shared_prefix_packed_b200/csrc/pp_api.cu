@@ -999,6 +999,8 @@ pp_status pp_get_status(void *stream) {
     e = cudaMemcpyToSymbol(pp::g_dev_err, &zero, sizeof(zero));
     if (e != cudaSuccess) return fail(PP_ERR_CUDA, "clearing the device error word: %s", cudaGetErrorString(e));
     if (word & pp::DEVERR_TIMEOUT) return fail(PP_ERR_DEVICE_TIMEOUT, "a kernel's bounded wait ran out (0x%x)", word);
+    if (word == pp::DEVERR_NO_ROOM)
+        return fail(PP_ERR_DEVICE_INPUT, "a resize of the paged cache needs more pages or slots than there are; it was not made (0x%x)", word);
     return fail(PP_ERR_DEVICE_INPUT, "inconsistent descriptors, segment boundaries, token ids or cache pages (0x%x)", word);
 }
 

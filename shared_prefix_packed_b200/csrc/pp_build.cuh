@@ -16,6 +16,7 @@ enum DevErr : int32_t {
     DEVERR_BAD_GROUPS = 4,     // descriptors disagree with the segments
     DEVERR_BAD_TOKEN = 8,      // a token id outside [0, V) given to pp_response_logprobs
     DEVERR_BAD_PAGES = 16,     // paged cache: lengths, page ids or slots that do not fit the pool or the table
+    DEVERR_NO_ROOM = 32,       // paged cache: a change that needs more pages or more slots than there are, and was not made
 };
 
 __device__ int32_t g_dev_err;  // this device's error word, read and cleared by pp_get_status

@@ -87,9 +87,9 @@ __global__ void __launch_bounds__(PAGES_THREADS) k_pages_resize(const PagesArgs 
     if (tid == 0) tok[a.nseg] = need[a.nseg] = back[a.nseg] = 0;
     __syncthreads();
     // 64-bit totals, so a sum past 2^31 is refused rather than wrapped
-    bool ok = !s_bad && n_free >= 0 && n_free <= a.num_pages && s_tok <= (unsigned long long)a.room &&
-                    s_back <= (unsigned long long)(a.num_pages - n_free) &&
-                    s_need <= (unsigned long long)n_free + s_back;
+    const bool fits = !s_bad && n_free >= 0 && n_free <= a.num_pages && s_back <= (unsigned long long)(a.num_pages - n_free);
+    bool ok = fits && s_tok <= (unsigned long long)a.room && s_need <= (unsigned long long)n_free + s_back;
+    int32_t err = fits ? DEVERR_NO_ROOM : DEVERR_BAD_PAGES;              // where it is not ok
     const int64_t nthreads = int64_t(cluster.num_blocks()) * PAGES_THREADS;
     const int64_t me = int64_t(cluster.block_rank()) * PAGES_THREADS + tid;
     int32_t R = ok ? int32_t(s_back) : 0, K = ok ? int32_t(s_need) : 0, NT = ok ? int32_t(s_tok) : 0;
@@ -116,6 +116,7 @@ __global__ void __launch_bounds__(PAGES_THREADS) k_pages_resize(const PagesArgs 
             for (unsigned r = 0; r < cluster.num_blocks(); ++r) out |= *cluster.map_shared_rank(&s_out, r) != 0;
             if (out) {
                 ok = false;
+                err = DEVERR_BAD_PAGES;
                 R = K = NT = 0;
             }
         }
@@ -128,7 +129,7 @@ __global__ void __launch_bounds__(PAGES_THREADS) k_pages_resize(const PagesArgs 
         a.counts[1] = K;
         a.counts[2] = R;
         a.counts[3] = ok ? 1 : 0;
-        if (!ok) set_dev_err(DEVERR_BAD_PAGES);
+        if (!ok) set_dev_err(err);
     }
     const int32_t top = n_free + R - 1;
     for (int64_t i = me; i < K; i += nthreads) {

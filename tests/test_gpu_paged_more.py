@@ -159,6 +159,21 @@ def test_resize_refuses_to_take_back_pages_outside_the_pool(new, bad):
     pp.pp_get_status()
 
 
+@pytest.mark.parametrize("new,n_free,capacity,word", [
+    ([3, 40, 100], 4, 99, "more pages or slots"), ([3, 40, 60], 7, 30, "more pages or slots"), ([3, -1, 20], 7, 99, "cache pages"),
+    ([3, 40, 100], 13, 99, "cache pages"), ([3, -1, 100], 4, 99, "cache pages"),
+])
+def test_resize_tells_a_full_pool_from_bad_input(new, n_free, capacity, word):
+    import shared_prefix_packed_b200 as pp
+    table = [[0] + [-1] * 7, [1, 2, 3] + [-1] * 5, [4, 5] + [-1] * 6]
+    free = [6, 7, 8, 9, 10, 11, 12, -5, -5, -5, -5, -5]
+    a = _resize_args([3, 40, 20], new, table, free, n_free, 16, capacity)
+    pp.pp_pages_resize(*a)
+    with pytest.raises(pp.PPError, match=f"DEVICE_INPUT.*{word}"):
+        pp.pp_get_status()
+    assert a[11].tolist() == [0] * 4 and a[8].tolist() == [n_free] and a[5].tolist() == table and a[6].tolist() == free
+
+
 @pytest.mark.parametrize("at", [None, 0, 1023, 1024, 5000, 8999])
 def test_resize_takes_back_many_pages_or_none(at):
     """9,000 pages given back, more than one CTA of the cluster looks at: all or, with one that does not fit, none."""
