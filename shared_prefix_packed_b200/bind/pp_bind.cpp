@@ -92,6 +92,11 @@ struct Call {
         need(x, what, dt, shape);
         return x;
     }
+    const Tensor &scratch(PyObject *o) {
+        const Tensor &x = *arg(o, "workspace");
+        if (!x.is_contiguous()) value_error("workspace must be contiguous");      // its bytes are those of its elements
+        return x;
+    }
     // The token stride of x [T, heads, d], whose heads and elements are dense.
     int64_t rows(const Tensor &x, const char *what, int64_t T, int64_t heads, int64_t d, ScalarType dt) {
         of_type(x, what, dt);
@@ -250,7 +255,7 @@ PyObject *norm_bwd(PyObject *const *a) {
     if (dwq) c.need(*dwq, "dwq", ScalarType::Float, {s.d});
     if (dwk) c.need(*dwk, "dwk", ScalarType::Float, {s.d});
     s.positions(c, a[4]);
-    const Tensor &ws = *c.arg(a[11], "workspace");
+    const Tensor &ws = c.scratch(a[11]);
     const float eps = number(a[12]), theta = number(a[13]);
     return c.run(a[14], [&](void *stream) {
         return g_norm_bwd(at_of(s.q), at_of(s.k), s.qs, s.ks, at_of(s.wq), at_of(s.wk), at_of<int32_t>(s.pos), s.T, s.hq, s.hkv, s.d,
@@ -339,7 +344,7 @@ PyObject *decode(PyObject *const *a) {
     c.need(q, "q", ScalarType::BFloat16, {n_resp, hq, p.d});
     const Tensor &o = c.need(a[9], "o", ScalarType::BFloat16, {n_resp, hq, p.d}), &lse = c.need(a[10], "lse", ScalarType::Float, {hq, n_resp});
     const Tensor &lens = c.need(a[7], "lens_d", ScalarType::Int, {g.nseg}), &table = c.need(a[8], "page_table_d", ScalarType::Int, {g.nseg, ANY});
-    const Tensor &ws = *c.arg(a[11], "workspace");
+    const Tensor &ws = c.scratch(a[11]);
     const float scale = number(a[12]);
     return c.run(a[13], [&](void *stream) {
         return g_decode(at_of(q), at_of(p.k), at_of(p.v), at_of<float>(p.ks), at_of<float>(p.vs), p.codes, p.num_pages, p.page,

@@ -1,0 +1,22 @@
+"""CPU checks of calls of the q/k norm and the paged cache that the first refusal tests leave out."""
+import pytest
+import torch
+
+from shared_prefix_packed_b200 import _lib
+
+
+def _cpu(*shape, dtype=torch.bfloat16):
+    return torch.zeros(*shape, dtype=dtype)
+
+
+@pytest.mark.parametrize("ws", [torch.zeros(1, dtype=torch.uint8).expand(1 << 20), torch.zeros(1 << 12, 2, dtype=torch.uint8)[:, 0]])
+def test_workspace_must_own_its_bytes(ws):
+    """A broadcast or strided tensor counts more bytes than it holds in one piece."""
+    kp, vp = _cpu(4, 2, 16, 128, dtype=torch.int8), _cpu(4, 2, 128, 16, dtype=torch.int8)
+    f = lambda *s: _cpu(*s, dtype=torch.float32)
+    i = lambda *s: _cpu(*s, dtype=torch.int32)
+    with pytest.raises(ValueError, match="workspace must be contiguous"):
+        _lib.pp_paged_decode(_cpu(2, 4, 128), kp, vp, f(4, 2), f(4, 2), i(2), i(3), i(3), i(3, 2), _cpu(2, 4, 128), f(4, 2), ws)
+    x = f(3, 4, 64)
+    with pytest.raises(ValueError, match="workspace must be contiguous"):
+        _lib.pp_qk_norm_rope_bwd(x, x, None, None, i(3), x, x, x, x, None, None, ws)
