@@ -13,7 +13,7 @@
  *   - Ownership: the caller owns all memory. The library allocates nothing on the device or the host (apart from a
  *     few small static tables of its own); every buffer is passed in as a raw pointer with its size.
  *   - Pointers: "_d" names and every tensor argument are DEVICE pointers on the current CUDA device, except where a
- *     comment says host. Tensors are dense and row-major:
+ *     comment says host, aligned to their elements where nothing more is asked. Tensors are dense and row-major:
  *       Q, O, dO, dQ: [T, Hq, d]; K, V, dK, dV: [T, Hkv, d]; LSE: [Hq, T] fp32; pos ids: int32 [T].
  *     The packed order is group by group: prefix, then the responses in order.
  *   - Asynchrony: every call only enqueues work on `stream` (a cudaStream_t; NULL = legacy default stream) and

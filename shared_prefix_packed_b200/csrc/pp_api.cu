@@ -200,6 +200,9 @@ pp_status noalloc_scratch(void **out) {
 
 bool bad_align(const void *p, int64_t a = 16) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
 
+// Arrays of int32 or float.
+template <typename... A> bool bad_words(const A *...p) { return (bad_align(p, 4) || ...); }
+
 // theta^(-2m/d) / (2 pi) in fp64, computed once per (theta, d) and thread.
 const pp::QknTurns &qkn_turns(float theta, int32_t d) {
     thread_local pp::QknTurns t;
@@ -806,6 +809,7 @@ pp_status pp_qk_norm_rope(const void *q, const void *k, int64_t q_stride, int64_
     if (st != PP_OK) return st;
     if (T == 0 || (!q && !k)) return PP_OK;
     if (!pos_ids_d) return fail(PP_ERR_INVALID_ARG, "pos_ids_d is NULL");
+    if (bad_words(pos_ids_d)) return fail(PP_ERR_INVALID_ARG, "pos_ids_d must be 4-byte aligned");
     const int64_t es = dt == PP_BF16 ? 2 : 4;
     const QknSide sq{q, wq, nullptr, q_out, q_stride, 0, qo_stride, hq}, sk{k, wk, nullptr, k_out, k_stride, 0, ko_stride, hkv};
     if ((st = qkn_check(sq, d, es, false, "q")) != PP_OK || (st = qkn_check(sk, d, es, false, "k")) != PP_OK) return st;
@@ -833,13 +837,14 @@ pp_status pp_qk_norm_rope_bwd(const void *q, const void *k, int64_t q_stride, in
     const QknSide sq{q, wq, gq, dq, q_stride, gq_stride, dq_stride, hq}, sk{k, wk, gk, dk, k_stride, gk_stride, dk_stride, hkv};
     if (T > 0) {
         if ((q || k) && !pos_ids_d) return fail(PP_ERR_INVALID_ARG, "pos_ids_d is NULL");
+        if (bad_words(pos_ids_d)) return fail(PP_ERR_INVALID_ARG, "pos_ids_d must be 4-byte aligned");
         if ((st = qkn_check(sq, d, es, true, "q")) != PP_OK || (st = qkn_check(sk, d, es, true, "k")) != PP_OK) return st;
     }
     const int64_t need = qkn_part_bytes(T, int64_t(q ? hq : 0) + (k ? hkv : 0), d);
     if (!workspace || ws_bytes < need)
         return fail(PP_ERR_WORKSPACE, "workspace %lld < %lld bytes", (long long)ws_bytes, (long long)need);
     if (bad_align(workspace, 256)) return fail(PP_ERR_INVALID_ARG, "workspace not 256-byte aligned");
-    if (bad_align(dwq, 4) || bad_align(dwk, 4)) return fail(PP_ERR_INVALID_ARG, "dwq and dwk must be 4-byte aligned");
+    if (bad_words(dwq, dwk)) return fail(PP_ERR_INVALID_ARG, "dwq and dwk must be 4-byte aligned");
     int32_t nq = 0, nk = 0;
     float *part = static_cast<float *>(workspace);
     if (T > 0 && (q || k) && (st = qkn_call<true>(sq, sk, pos_ids_d, T, d, eps, theta, dt, part, &nq, &nk, s)) != PP_OK)
@@ -865,6 +870,9 @@ pp_status pp_pages_resize(const int32_t *group_start_d, int32_t G, const int32_t
     if (!group_start_d || !seg_group_d || !old_lens_d || !new_lens_d || !page_table_d || !free_pages_d || !n_free_in ||
         !n_free_out || !counts_d || (capacity > 0 && (!slots_d || !pos_ids_d)))
         return fail(PP_ERR_INVALID_ARG, "NULL pointer argument");
+    if (bad_words(group_start_d, seg_group_d, old_lens_d, new_lens_d, page_table_d, free_pages_d, n_free_in, n_free_out, slots_d,
+                  pos_ids_d, counts_d))
+        return fail(PP_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
     DeviceInfo *di;
     if ((st = device_info(&di)) != PP_OK) return st;
     const pp::PagesArgs a{group_start_d, seg_group_d, old_lens_d, new_lens_d, page_table_d, free_pages_d, n_free_in,
@@ -906,6 +914,7 @@ pp_status pp_cache_store(const void *k, const void *v, int64_t k_stride, int64_t
         return fail(PP_ERR_INVALID_ARG, "row stride below hkv * d");
     if (bad_align(k) || bad_align(v) || bad_align(k_pages) || bad_align(v_pages) || k_stride * es % 16 || v_stride * es % 16)
         return fail(PP_ERR_INVALID_ARG, "k, v, pages and row strides must be multiples of 16 bytes");
+    if (bad_words(slots_d, k_scale, v_scale)) return fail(PP_ERR_INVALID_ARG, "slots_d and scales must be 4-byte aligned");
     DeviceInfo *di;
     if ((st = device_info(&di)) != PP_OK) return st;
     auto go = dt == PP_BF16 ? store_rows<__nv_bfloat16> : store_rows<float>;
@@ -944,6 +953,8 @@ pp_status pp_paged_decode(const void *q, const void *k_pages, const void *v_page
         return fail(PP_ERR_INVALID_ARG, "NULL pointer argument");
     if (bad_align(q) || bad_align(k_pages) || bad_align(v_pages) || bad_align(o))
         return fail(PP_ERR_INVALID_ARG, "q, pages and o must be 16-byte aligned");
+    if (bad_words(k_scale, v_scale, group_start_d, seg_group_d, lens_d, page_table_d, lse))
+        return fail(PP_ERR_INVALID_ARG, "scales, descriptors, lens_d, page_table_d and lse must be 4-byte aligned");
     int64_t need = 0;
     if ((st = pp_paged_decode_bytes(n_resp, hq, hkv, &need)) != PP_OK) return st;
     if (!workspace || ws_bytes < need)

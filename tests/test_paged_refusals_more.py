@@ -3,6 +3,7 @@ import pytest
 import torch
 
 from shared_prefix_packed_b200 import _lib
+from tests.test_paged_refusals import BWD, DECODE, NORM, P, RESIZE, STORE, _call
 
 
 def _cpu(*shape, dtype=torch.bfloat16):
@@ -20,3 +21,18 @@ def test_workspace_must_own_its_bytes(ws):
     x = f(3, 4, 64)
     with pytest.raises(ValueError, match="workspace must be contiguous"):
         _lib.pp_qk_norm_rope_bwd(x, x, None, None, i(3), x, x, x, x, None, None, ws)
+
+
+@pytest.mark.parametrize("name,base,args", [
+    ("pp_qk_norm_rope", NORM, ["pos"]),
+    ("pp_qk_norm_rope_bwd", BWD, ["pos", "dwq", "dwk"]),
+    ("pp_pages_resize", RESIZE, ["gs", "sg", "old", "new", "table", "free", "nin", "nout", "slots", "pos", "counts"]),
+    ("pp_cache_store", STORE, ["slots", "ksc", "vsc"]),
+    ("pp_paged_decode", DECODE, ["ksc", "vsc", "gs", "sg", "lens", "table", "lse"]),
+])
+def test_words_must_be_aligned(name, base, args):
+    """An int32 or float array at an address that the GPU could not read it from."""
+    for arg in args:
+        for off in (1, 2):
+            st, msg = _call(name, base, **{arg: P + off})
+            assert st == "PP_ERR_INVALID_ARG" and "4-byte aligned" in msg, (arg, msg)
