@@ -294,10 +294,15 @@ def _done(name, st):
 
 def stream_scope(device, stream):
     """A context in which torch allocates and launches on `stream` (None: the device's current stream), so that
-    scratch and outputs belong to the stream that uses them."""
+    scratch and outputs belong to the stream that uses them. Raises ValueError for a stream of another device, whose
+    scope would leave this device's own current stream in place."""
     torch = _torch()
     if stream is None:
         return torch.cuda.stream(None)                     # does nothing
+    if not isinstance(stream, int):
+        at = torch.cuda.current_device() if device.index is None else device.index
+        if stream.device.index != at:
+            raise ValueError(f"the stream is of cuda:{stream.device.index}, the tensors of cuda:{at}")
     return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream)
 
 

@@ -36,3 +36,12 @@ def test_words_must_be_aligned(name, base, args):
         for off in (1, 2):
             st, msg = _call(name, base, **{arg: P + off})
             assert st == "PP_ERR_INVALID_ARG" and "4-byte aligned" in msg, (arg, msg)
+
+
+def test_streams_of_another_device():
+    """The calls that allocate for themselves refuse them, as the plain calls do."""
+    class Stream:
+        device, cuda_stream = torch.device("cuda:1"), 0
+
+    with pytest.raises(ValueError, match="the stream is of cuda:1, the tensors of cuda:0"):
+        _lib.stream_scope(torch.device("cuda:0"), Stream())
