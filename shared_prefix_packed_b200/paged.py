@@ -50,6 +50,7 @@ class PagedCache:
         self.free_pages = torch.arange(num_pages - 1, -1, -1, **i32)     # taken from its end: page 0 first
         self.n_free = torch.tensor([num_pages], **i32)
         self.lens = torch.zeros(self.num_segments, **i32)
+        self.device = self.lens.device                       # "cuda" is the device of now, not of each later call
 
     def resize(self, new_lens, capacity: int | None = None, stream=None):
         """Bring the segments to new_lens tokens (a sequence, or an int32 tensor on the device): pages are taken for

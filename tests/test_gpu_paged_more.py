@@ -75,6 +75,19 @@ def test_decode_queries_at_the_ends_of_bf16(top, k_exp):
     assert np.all(np.abs(a[10].double().cpu().numpy() - want[1]) <= bl)
 
 
+def test_cache_keeps_its_device():
+    """A cache made on "cuda" stays on the device that was current then."""
+    import shared_prefix_packed_b200 as pp
+    cache = pp.PagedCache([1], 4, 2, 4, 64)
+    assert cache.device == cache.k_pages.device == torch.device("cuda", torch.cuda.current_device())
+    for stream in (None, torch.cuda.Stream(), torch.cuda.Stream().cuda_stream):
+        slots, pos, counts = cache.resize([5, 3], stream=stream)
+        torch.cuda.synchronize()
+        assert slots.device == cache.device and counts[3] == 1
+        cache.resize([0, 0], stream=stream)
+        torch.cuda.synchronize()
+
+
 # ------------------------------------------------------------------------------------------------------------- append
 def _rows(rng, n, heads, dtype):
     """Rows of far-apart sizes, so that each decides a scale of its own."""
