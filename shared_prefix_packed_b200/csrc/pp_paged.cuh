@@ -47,27 +47,18 @@
 #include <cuda_runtime.h>
 #include "pp_attn_fwd.cuh"  // bwait
 #include "pp_cache.cuh"
+#include "pp_paged_shares.cuh"
 #include "pp_pages.cuh"     // PAGES_MAX_SEGS
 #include "pp_ptx.cuh"
 
 namespace pp {
 
-constexpr int PD_CH = 64;             // keys of a job
-constexpr int PD_RB = 16;             // query rows of a job, at most
-constexpr int PD_WARPS = 12;
 constexpr int PD_BATCH = 16;          // jobs that a warp decodes at a time
 constexpr int PD_THREADS = PD_WARPS * 32;
-constexpr int PD_MAX_CTAS = 148;      // what a workspace is sized for
 constexpr int PD_RUNS = 2048;         // runs of segments that a block keeps the sums before: of 1, 2 or 4 segments
 static_assert(4 * PD_RUNS >= PAGES_MAX_SEGS, "runs");
 constexpr float PD_OFF = 7.f;         // p = 2^(x - max + 7) at the maximum
 constexpr float PD_LAZY = 8.f;        // the maximum may be exceeded by this before the sums are rescaled
-
-// What a job costs, in units that the warps' shares are equal in: one of up to 8 query rows, one of up to 16, and the
-// first of an item more (its queries and its record). Measured on 16 groups of 8 responses (prefixes of 256 to 1024
-// tokens, 64 to 2048 of their own) and 17 of 4 (to 16384 and 4096), 32 / 8 heads: with equal numbers of jobs 64.4 and 86.4
-// us, with 2, 3 and 1 units 56.3 and 80.7, with 2, 3, 2 57.3 and 81.0, with 2, 3, 3 56.8 and 81.3, with 1, 2, 2 58.7 and 91.4.
-constexpr int PD_COST8 = 2, PD_COST16 = 3, PD_COST_ITEM = 1;
 
 struct alignas(16) PagedSegRec {
     int32_t off;                               // units before the segment
@@ -95,7 +86,7 @@ struct PagedWorkspace {
     int64_t off_seg, off_ml, off_part, total;
 };
 __host__ inline PagedWorkspace paged_workspace(int32_t n_resp, int32_t hq) {
-    const int64_t rows = 2 * int64_t(n_resp) * hq + int64_t(PD_MAX_CTAS) * PD_WARPS * PD_RB;
+    const int64_t rows = paged_rows(n_resp, hq);
     auto up = [](int64_t x) { return (x + 255) & ~int64_t(255); };
     PagedWorkspace w{};
     w.off_seg = 256;
@@ -136,38 +127,6 @@ __device__ __forceinline__ PagedSeg paged_seg(const PagedArgs &a, int s) {
     return d;
 }
 __device__ __forceinline__ int paged_run_log2(const PagedArgs &a) { return a.nseg <= PD_RUNS ? 0 : a.nseg <= 2 * PD_RUNS ? 1 : 2; }
-// Units of one item, and before its job k.
-__device__ __forceinline__ int32_t paged_cost(int32_t qrows) { return qrows <= 8 ? PD_COST8 : PD_COST16; }
-__device__ __forceinline__ int32_t paged_item(int32_t nch, int32_t qrows) {
-    return nch ? PD_COST_ITEM + nch * paged_cost(qrows) : 0;
-}
-__device__ __forceinline__ int32_t paged_start(int32_t k, int32_t qrows) {
-    return k ? PD_COST_ITEM + k * paged_cost(qrows) : 0;
-}
-// First record row of a segment's items, without the warp's part: prefixes and responses in order, each hq rows for
-// every response that sees it.
-__device__ __forceinline__ int32_t paged_row(const PagedArgs &a, const PagedSeg &d) {
-    return (d.prefix ? 2 * d.r0 : d.r0 + d.kg + d.qbase) * a.hq;
-}
-
-// The shares of n units among up to `warps` warps: a job is its warp's whose share holds its first unit. As many warps
-// take part as leave each the units of the longest job, so every one of them has a job, and the warps that have a part
-// of an item follow one another.
-struct PagedShare {
-    int32_t many, per, more;                               // warps, units of a warp, warps with one more
-    __device__ PagedShare(int32_t n, int32_t warps) {
-        many = max(1, min(warps, n / (PD_COST_ITEM + PD_COST16)));
-        per = n / many;
-        more = n - per * many;
-    }
-    __device__ explicit PagedShare(int4 total) : many(total.y), per(total.z), more(total.w) {}
-    __device__ int32_t begin(int32_t w) const { return w >= many ? per * many + more : per * w + min(w, more); }
-    __device__ int32_t warp_of(int32_t u) const {
-        const int32_t cut = more * (per + 1);
-        const bool low = u < cut;
-        return (low ? 0 : more) + int32_t(uint32_t(low ? u : u - cut) / uint32_t(low ? per + 1 : per));
-    }
-};
 
 // Four codes to two f16 pairs, exactly.
 template <int FMT> __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t &a, uint32_t &b) {
@@ -471,9 +430,7 @@ __device__ __forceinline__ int32_t paged_job_at(const PagedArgs &a, const int32_
     const int32_t qrows = (p.prefix ? p.kg : 1) * a.r, cost = paged_cost(qrows);
     const uint32_t item = paged_item(p.nch, qrows), i = p.within / item;
     const int32_t rest = p.within - i * item + (u >= n_units);           // past the last unit: after the last job
-    // job k > 0 begins at PD_COST_ITEM + k cost
-    const int32_t k = rest == 0 ? 0 : max(1, (rest - PD_COST_ITEM + cost - 1) / cost);
-    return p.before + int32_t(i) * p.nch + k;
+    return p.before + int32_t(i) * p.nch + paged_job_from(rest, cost);
 }
 // Jobs base ... base + PD_BATCH - 1 of a warp's: what they are (a lane a job), then their pages (a lane two of the 4 x 16
 // sixteens of keys).
@@ -495,7 +452,7 @@ static __device__ __noinline__ void paged_decode_jobs(const PagedArgs &a, PagedJ
         const uint32_t first = uint32_t(rho) / uint32_t(a.r);
         e.resp = qbase + first;
         e.hh = rho - first * a.r;
-        e.rec = (p.prefix ? 2 * p.r0 : p.r0 + p.kg + qbase) * a.hq + head * qrows + rho + who * PD_RB;     // paged_row
+        e.rec = paged_row(p.prefix, p.r0, p.kg, qbase, a.hq) + head * qrows + rho + who * PD_RB;
     }
     __syncwarp();
     int32_t id[2];
@@ -578,7 +535,7 @@ k_paged_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         }
         const int32_t item = paged_item(d.nch, d.qrows);
         if (lister)
-            a.seg[s] = PagedSegRec{int32_t(units), item, paged_start(d.nch - 1, d.qrows), d.nblk, paged_row(a, d), d.qrows, d.qbase,
+            a.seg[s] = PagedSegRec{int32_t(units), item, paged_start(d.nch - 1, d.qrows), d.nblk, paged_row(d.prefix, d.r0, d.kg, d.qbase, a.hq), d.qrows, d.qbase,
                                    d.ok && !d.prefix ? s - d.place : -1};
         const int32_t items = d.nblk * a.hkv;
         jobs += int64_t(d.nch) * items;
@@ -752,7 +709,7 @@ __global__ void __launch_bounds__(PD_COMB_WARPS * 32) k_paged_combine(const Page
         // lanes 0 and 1: the first warp with a part of the item, lanes 2 and 3: the last
         const int kh = int((float(h) + 0.5f) * a.inv_r), rho = (resp - d.qbase) * a.r + (h - kh * a.r);
         const int32_t u = d.off + (kh * d.nblk + rho / PD_RB) * d.item + (lane & 2 ? d.last : 0);
-        const int32_t who = d.item > 0 ? PagedShare(all).warp_of(u) + (lane & 2 ? 1 : 0) : 0;
+        const int32_t who = d.item > 0 ? PagedShare(all.y, all.z, all.w).warp_of(u) + (lane & 2 ? 1 : 0) : 0;
         const int32_t at = d.row + kh * d.qrows + rho + who * PD_RB;   // record row of the first piece, which it is for lanes 0 and 1
         int64_t row[2];
         int n[2];
