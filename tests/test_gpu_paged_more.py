@@ -75,6 +75,44 @@ def test_decode_queries_at_the_ends_of_bf16(top, k_exp):
     assert np.all(np.abs(a[10].double().cpu().numpy() - want[1]) <= bl)
 
 
+def test_decode_many_jobs_to_a_warp():
+    """83,616 jobs, some 47 to each of 1776 warps, so that every warp decodes its jobs in three or four lots of 16; jobs of
+    up to 8 and of up to 16 query rows, items that end inside a lot, that are cut between warps, and of one job."""
+    import shared_prefix_packed_b200 as pp
+    num, lens, page, r, hkv = [3, 1], [60000, 30000, 7, 12000, 45000, 20000], 128, 4, 32
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    pages = [-(-n // page) for n in lens]
+    total = sum(pages)
+    k, v = (torch.randint(-127, 128, s, generator=gen, device="cuda", dtype=torch.int8) for s in ((total, hkv, page, 128), (total, hkv, 128, page)))
+    sk, sv = (2.0 ** torch.randint(lo, lo + 3, (total, hkv), generator=gen, device="cuda").float() for lo in (-8, -6))
+    ids, at = torch.randperm(total, generator=gen, device="cuda").to(torch.int32), 0
+    table = torch.full((len(lens), max(pages)), -1, dtype=torch.int32, device="cuda")
+    for s, n in enumerate(pages):
+        table[s, :n] = ids[at:at + n]
+        at += n
+    t = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    q = torch.randn(4, r * hkv, 128, generator=gen, device="cuda").to(torch.bfloat16)
+    o, lse = torch.empty_like(q), torch.empty(r * hkv, 4, device="cuda")
+    ws = torch.empty(pp.pp_paged_decode_bytes(4, r * hkv, hkv), dtype=torch.uint8, device="cuda")
+    pp.pp_paged_decode(q, k, v, sk, sv, t([0, 4, 6]), t([0] * 4 + [1] * 2), t(lens), table, o, lse, ws)
+    pp.pp_get_status()
+    for i, segs in enumerate(((0, 1), (0, 2), (0, 3), (4, 5))):
+        place = [(table[s].long()[torch.arange(lens[s], device="cuda") // page], torch.arange(lens[s], device="cuda") % page) for s in segs]
+        pg, off = (torch.cat(x) for x in zip(*place))
+        for h in range(hkv):
+            kk = k[pg, h, off].double() * sk[pg, h][:, None].double()
+            vv = v[pg, h, :, off].double() * sv[pg, h][:, None].double()
+            qq = q[i, r * h:r * h + r].double()
+            x = qq @ kk.T / 128 ** 0.5
+            z = torch.logsumexp(x, -1)
+            p = torch.exp(x - z[:, None])
+            size = (qq.abs() @ kk.abs().T / 128 ** 0.5).amax(-1)
+            want, spread = p @ vv, p @ vv.abs()
+            bo, bl = decode_bounds(*(y.cpu().numpy() for y in (want, z, spread, size)), sum(lens), 6)
+            got, got_l = o[i, r * h:r * h + r].double(), lse[r * h:r * h + r, i].double()
+            assert np.all((got - want).abs().cpu().numpy() <= bo) and np.all((got_l - z).abs().cpu().numpy() <= bl)
+
+
 def test_cache_keeps_its_device():
     """A cache made on "cuda" stays on the device that was current then."""
     import shared_prefix_packed_b200 as pp
