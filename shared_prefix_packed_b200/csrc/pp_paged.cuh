@@ -681,11 +681,16 @@ k_paged_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
 
 // The outputs of a response from the records of its prefix's items and of its own, one for each warp that had a share of
 // an item. Eight warps to a block, a lane four of the 128 outputs. ALONE: a warp takes a q head; otherwise a block takes
-// one and its warps deal the records out. Items are at least heads / 16, so the shares cut one into at most
-// 16 * warps / heads + 2 records: with more than PD_COMB_ALONE heads in all that is 14, a short chain of loads for one
-// warp, and with fewer there is room for a block each. Measured, both kernels: 16 responses of 28 heads behind prefixes of
-// up to 8192 tokens, a block a head 28.4 us and a warp a head 50.3; 68 of 32 heads 77.7 and 81.6; 128 of 32 heads 62.8 and
-// 56.4. Bound by latency: the shares, a record's two numbers, its outputs.
+// one and its warps deal the records out. A block a head shortens the chain of records where a head has many; a warp a head
+// needs an eighth of the blocks. Which of the two it is goes by the heads in all, as the host does not know the lengths:
+// with equal responses the warps cut an item into 16 * warps / heads + 2 records on average, 14 above PD_COMB_ALONE heads.
+// Measured, both kernels, L2 flushed, a block a head and a warp a head (32 / 8 heads; groups of 8 responses of 600 tokens behind
+// 500): 1024 heads 36.9 and 38.9 us, 2048 49.2 and 47.1, 2304 51.2 and 49.2, 2560 57.3 and 53.2, 4096 73.7 and 67.6; unlike lengths, to 16384
+// (2176 heads, calls in a row) 80.3 and 87.8; 448 heads behind 6000 tokens 38.9 and 57.3; 8192 heads of 20 tokens 53.2 and 36.9. The rule
+// does not see one long response among many short: behind 131,072 tokens beside 126 of 100 (4064 heads) its heads have some
+// 180 records each, and a warp a head takes 139 us where a block takes 98; behind 32,768, 86 and 57. (Dealing such a head out
+// to its block's warps, whose other heads are as long: 121 and 72, and 0.5 us more elsewhere.) Bound by latency: the shares, a
+// record's two numbers, its outputs.
 constexpr int PD_COMB_WARPS = 8, PD_COMB_ALONE = 2304;
 template <bool ALONE>
 __global__ void __launch_bounds__(PD_COMB_WARPS * 32) k_paged_combine(const PagedArgs a) {

@@ -243,3 +243,22 @@ def test_resize_takes_back_many_pages_or_none(at):
             pp.pp_get_status()
         assert a[11].tolist() == [0] * 4 and a[6].tolist() == free and a[8].item() == 0
     assert a[5].tolist() == table.tolist()
+
+
+@pytest.mark.parametrize("hq,hkv", [(32, 8), (28, 4)])
+def test_decode_one_long_response_among_many_short(hq, hkv):
+    """More than 2304 heads in all, so a warp of the second kernel takes a head, of which some have many records: a long
+    prefix with one response, a long response behind a short prefix, responses of nothing beside them."""
+    num = [1, 2] + [7] * 12
+    lens = [9000, 40, 64, 7000, 0] + [x for _ in range(12) for x in [33] + [20, 0, 64, 65, 1, 130, 7]]
+    c = random_cache(num, lens, 64, hkv, "int8", 12)
+    n = sum(num)
+    assert n * hq > 2304
+    a = _decode_args(c, hq, 4)
+    _call_decode(a)
+    q = a[0]
+    want = pc.decode(q.double().cpu().numpy(), c["k_vals"], c["v_vals"], c["k_scale"].astype(np.float64),
+                     c["v_scale"].astype(np.float64), num, lens, c["table"])
+    bo, bl = decode_bounds(*want, n_keys=sum(lens), scale_exp=7)
+    assert np.all(np.abs(a[9].double().cpu().numpy() - want[0]) <= bo)
+    assert np.all(np.abs(a[10].double().cpu().numpy() - want[1]) <= bl)
