@@ -70,7 +70,8 @@ class PagedCache:
             slots, pos, counts = torch.empty(capacity, **i32), torch.empty(capacity, **i32), torch.empty(4, **i32)
             _lib.pp_pages_resize(self.group_start, self.seg_group, self.lens, new, self.page_size, self.page_table,
                                  self.free_pages, self.n_free, self.n_free, slots, pos, counts)
-            self.lens.copy_(torch.where(counts[3] > 0, new, self.lens))
+            # counts[3] is 0 or 1: its first byte is that truth value, so that this is one launch
+            torch.where(counts.view(torch.bool)[12], new, self.lens, out=self.lens)
         return slots, pos, counts
 
     def append(self, k, v, slots, stream=None):

@@ -262,3 +262,27 @@ def test_decode_one_long_response_among_many_short(hq, hkv):
     bo, bl = decode_bounds(*want, n_keys=sum(lens), scale_exp=7)
     assert np.all(np.abs(a[9].double().cpu().numpy() - want[0]) <= bo)
     assert np.all(np.abs(a[10].double().cpu().numpy() - want[1]) <= bl)
+
+
+def test_cache_lengths_follow_only_changes_that_are_made():
+    """PagedCache.lens after a change that is made, one that is refused, and one captured into a graph of which both are
+    replayed; the lengths given are not written to."""
+    import shared_prefix_packed_b200 as pp
+    cache = pp.PagedCache([2], 4, 2, 6, 64, 16)
+    new = torch.tensor([20, 3, 1], dtype=torch.int32, device="cuda")
+    assert cache.resize(new, 64)[2].tolist() == [24, 4, 0, 1] and cache.lens.tolist() == [20, 3, 1]
+    assert cache.resize([20, 40, 40], 64)[2].tolist() == [0] * 4 and cache.lens.tolist() == [20, 3, 1]      # 7 pages
+    with pytest.raises(pp.PPError, match="more pages or slots"):
+        pp.pp_get_status()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        counts = cache.resize(new, 64)[2]
+    for lens, made in (([20, 17, 1], True), ([50, 50, 50], False), ([0, 17, 33], True), ([0, 0, 0], True)):
+        was = cache.lens.tolist()
+        new.copy_(torch.tensor(lens, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert counts[3].item() == made and cache.lens.tolist() == (lens if made else was) and new.tolist() == lens
+    assert cache.n_free.item() == 6
+    with pytest.raises(pp.PPError, match="more pages or slots"):
+        pp.pp_get_status()
