@@ -232,7 +232,8 @@ PP_API pp_status pp_decode_attn(const void *q, const void *k_cache, const void *
  * pp_qk_norm_rope: RMS norm of every query and key head and the rotation of pp_rope in one pass.
  *   r = (mean_i x_i^2 + eps)^-1/2 over a row of d elements (one token, one head); z_i = x_i r w_i; the row is then
  *   rotated at the token's position as by pp_rope (inverse = 0). The norm is formed in fp32, the angle in fp64, and
- *   the result is rounded once, to nearest even.
+ *   the result is rounded once, to nearest even. Squares and their sum are fp32: a row whose sum passes its range (elements
+ *   of some 10^18 and more) gives zeros; with eps = 0 rows of elements below 10^-19 lose bits, and zeros give NaN.
  *   q: T tokens of [hq, d], k: T tokens of [hkv, d], dt PP_BF16 or PP_FP32; q_stride and k_stride are the elements
  *   from one token to the next (hq * d and hkv * d for a dense tensor; more for the heads of a fused projection), a
  *   multiple of 16 bytes. q_out, k_out likewise with qo_stride, ko_stride; an output may be its input (same pointer

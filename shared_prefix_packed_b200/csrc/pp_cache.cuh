@@ -26,8 +26,8 @@ constexpr int CACHE_D = 128;
 constexpr int CACHE_E_MIN = -40, CACHE_E_MAX = 56;   // every ratio of two scales stays far inside fp32's range
 constexpr int CACHE_THREADS = 256;
 // Rows of a run that one warp takes. Measured with 128 and 512 runs of 1, 2, 4 and 8 bf16 rows, 8 heads, pages of 64: up
-// to 4 rows 7.5, 7.4, 9.9, 15.7 and 14.5, 18.8, 38.3, 52.6 us; up to 8 rows (longer code, more registers) 8.6, 8.9, 12.2,
-// 20.3 and 17.4, 23.1, 40.9, 53.6; single rows only 7.1, 11.9, 12.5, 15.8 and 14.3, 35.0, 48.1, 52.4.
+// to 4 rows 7.0, 8.0, 12.0, 17.5 and 14.8, 20.1, 44.7, 57.5 us; up to 8 rows (longer code) 7.0, 8.3, 11.7, 18.8 and 15.6,
+// 21.4, 46.0, 59.4; single rows only 6.6, 12.1, 13.6, 17.0 and 14.6, 36.0, 51.5, 55.8.
 constexpr int CACHE_SHORT = 4;
 constexpr int CACHE_APART = 256;      // rows of a page are one append if each is at most this many rows after the one before
 
@@ -221,7 +221,8 @@ static __device__ __noinline__ void cache_look_apart(const int32_t *slots, int64
 
 // A page's rows that are not one run: from row i0 on, skipped rows and rows in any order among them, up to the last that
 // follows the one before within CACHE_APART rows with no other page's row between. The whole block, a warp a row, each row
-// read twice: no caller of pp_pages_resize has such rows. s_row: 128 ints, s_red: 8 words, both free on entry.
+// read twice: ten times as slow as a run (a row left out of each of 1386 pages of 64, 8 heads: 1084 us, whole pages 103), but
+// slots of pp_pages_resize are runs. s_row: 128 ints, s_red: 8 words, both free on entry.
 template <typename T, int FMT>
 static __device__ __noinline__ void cache_store_apart(const T *rows, int64_t stride, const int32_t *slots, int64_t n, int64_t i0, int lg,
                                                       int32_t num_pages, int hkv, bool val, int h0, int h1, uint8_t *pages,
@@ -312,8 +313,8 @@ static __device__ __noinline__ void cache_store_apart(const T *rows, int64_t str
 // or warp therefore owns. Nearly always it is a run, slots that ascend by one row by row; what is not goes to
 // cache_store_apart. Runs of up to CACHE_SHORT rows (an appended token) go to a warp each; longer ones to the whole block,
 // rows held in registers between the maximum and the codes, so that every row is read once, and the next head's rows
-// asked for before this one's codes are written. A decode step (128 rows of 8 heads, 6.1 us) is bound by latency: slots,
-// rows and scale, codes. A prefill (88,685 bf16 rows of 8 heads, 545 MB read and written in 122 us: 4.5 TB/s, 68 % of a
+// asked for before this one's codes are written. A decode step (128 rows of 8 heads, 6.5 us) is bound by latency: slots,
+// rows and scale, codes. A prefill (88,685 bf16 rows of 8 heads, 545 MB read and written in 125 us: 4.4 TB/s, 67 % of a
 // plain copy's rate) by what stands between the loads: the block's maximum and its barriers, with 29 warps to an SM and
 // two thirds of the issue slots taken. (The next head's rows asked for before the maximum, at 80 registers a thread and
 // three blocks to an SM: 144 us.)
