@@ -377,7 +377,7 @@ __device__ __forceinline__ void paged_record(PagedItem<NB> &it, const PagedArgs 
             const int n = 8 * h + 2 * c + e;
             if (n < nrows) {
                 const int64_t row = int64_t(rec) + n;
-                if (g == 0) a.ml[row] = make_float2(it.m[h][e] == -INFINITY ? 0.f : it.m[h][e], l);
+                if (g == 0) a.ml[row] = make_float2(it.m[h][e], l);       // -inf: no key gave a number above it
                 float *dst = a.part + row * CACHE_D + g;
 #pragma unroll
                 for (int t = 0; t < 8; ++t) {

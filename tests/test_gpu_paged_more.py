@@ -75,6 +75,37 @@ def test_decode_queries_at_the_ends_of_bf16(top, k_exp):
     assert np.all(np.abs(a[10].double().cpu().numpy() - want[1]) <= bl)
 
 
+def test_decode_scores_beyond_fp32_beside_low_ones():
+    """A segment whose scores all pass fp32's range to -inf weighs nothing, however low the other segment's scores are; alone it
+    has no softmax."""
+    import shared_prefix_packed_b200 as pp
+    page, n = 64, 64
+    vals = np.zeros((2, 1, page, 128))
+    vals[0, 0, :, 1] = np.arange(64) / 8 + 24                # the prefix: scores of some -1300
+    vals[1, 0, :, 0] = -448                                  # the response: below -2^128
+    k = torch.from_numpy(vals).float().to(torch.float8_e4m3fn).cuda()
+    v_vals = np.random.default_rng(1).integers(-8, 9, (2, 1, 128, page)).astype(np.float64)
+    v = torch.from_numpy(v_vals).float().to(torch.float8_e4m3fn).cuda()
+    sk, sv = torch.tensor([[2.0 ** -106], [1.0]], device="cuda"), torch.ones(2, 1, device="cuda")
+    t = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    q = torch.zeros(1, 1, 128, dtype=torch.bfloat16, device="cuda")
+    q[0, 0, 0], q[0, 0, 1] = 2.0 ** 127, -2.0 ** 115
+    o, lse = torch.empty_like(q), torch.empty(1, 1, device="cuda")
+    ws = torch.empty(pp.pp_paged_decode_bytes(1, 1, 1), dtype=torch.uint8, device="cuda")
+    for lens, seen in (([n, n], True), ([n, 0], True), ([0, n], False)):
+        pp.pp_paged_decode(q, k, v, sk, sv, t([0, 2]), t([0, 0]), t(lens), t([[0], [1]]), o, lse, ws)
+        pp.pp_get_status()
+        if not seen:
+            assert torch.isnan(o.float()).all() and torch.isneginf(lse).all()
+            continue
+        x = -(2.0 ** 9) * k[0, 0, :, 1].float().double().cpu().numpy() / 128 ** 0.5
+        z = np.max(x) + np.log(np.sum(np.exp(x - np.max(x))))
+        p = np.exp(x - z)
+        want, spread = v_vals[0, 0] @ p, np.abs(v_vals[0, 0]) @ p
+        bo, bl = decode_bounds(want[None, None], np.array([[z]]), spread[None, None], np.array([[np.max(np.abs(x))]]), n, 1)
+        assert np.all(np.abs(o.double().cpu().numpy() - want) <= bo) and np.abs(lse.item() - z) <= bl[0, 0]
+
+
 def test_decode_many_jobs_to_a_warp():
     """83,616 jobs, some 47 to each of 1776 warps, so that every warp decodes its jobs in three or four lots of 16; jobs of
     up to 8 and of up to 16 query rows, items that end inside a lot, that are cut between warps, and of one job."""
@@ -286,3 +317,33 @@ def test_cache_lengths_follow_only_changes_that_are_made():
     assert cache.n_free.item() == 6
     with pytest.raises(pp.PPError, match="more pages or slots"):
         pp.pp_get_status()
+
+
+def test_rollout_from_lists_of_lengths():
+    """A prefill and single steps with the lengths as lists: the rows are as many as the capacity, which by default is the
+    sum of the lengths, and a step names it."""
+    import shared_prefix_packed_b200 as pp
+    hq, hkv = 8, 2
+    cache = pp.PagedCache([2, 3], hq=hq, hkv=hkv, num_pages=40, max_tokens=256)
+    wq, wk = (torch.ones(128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    lens = [100, 0, 0, 70, 0, 0, 0]
+
+    def put(slots, pos):
+        n = slots.numel()
+        x = torch.randn(n, hq + 2 * hkv, 128, device="cuda").to(torch.bfloat16)
+        q, k = torch.empty(n, hq, 128, dtype=x.dtype, device="cuda"), torch.empty(n, hkv, 128, dtype=x.dtype, device="cuda")
+        pp.pp_qk_norm_rope(x[:, :hq], x[:, hq:hq + hkv], wq, wk, pos, q, k)
+        cache.append(k, x[:, hq + hkv:], slots)
+        return q
+
+    slots, pos, counts = cache.resize(lens)
+    assert slots.numel() == 170 and counts.tolist() == [170, 4, 0, 1]
+    put(slots, pos)
+    for _ in range(3):
+        lens = [n + (i not in (0, 3)) for i, n in enumerate(lens)]
+        slots, pos, counts = cache.resize(lens, capacity=5)
+        q = put(slots, pos)
+        o, lse = cache.decode(q)
+        assert counts.tolist()[0] == 5 and torch.isfinite(o.float()).all() and torch.isfinite(lse).all()
+    assert pos.tolist() == [102, 102, 72, 72, 72]
+    pp.pp_get_status()
