@@ -264,7 +264,7 @@ static __device__ __noinline__ void cache_store_apart(const T *rows, int64_t str
     }
     __syncthreads();
     int o0 = 0;
-    while (s_row[o0] < 0) ++o0;                           // row i0 has one
+    while (o0 < page - 1 && s_row[o0] < 0) ++o0;           // row i0 has one
     auto load = [&](int64_t t, int h, float (&x)[4]) {    // a lane four elements
         const T *row = rows + t * stride + h * CACHE_D + 4 * lane;
 #pragma unroll
