@@ -9,8 +9,9 @@
 // nothing in range or precision; int8 gives up at most one of its 8 bits.
 //
 // The rows of one page that stand together in a call are one append, whatever the order and the gaps of their slots: one
-// owner forms their one scale. Appending to a page that already holds tokens keeps the larger of its scale and the one that the new rows need; if
-// it grows, the codes already there are re-rounded to it. Values that are not finite do not count for the scale.
+// owner forms their one scale. Appending to a page that already holds tokens keeps the larger of its scale and the one that
+// the new rows need; if it grows, the codes already there are re-rounded to it. Values that are not finite do not count for
+// the scale.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
